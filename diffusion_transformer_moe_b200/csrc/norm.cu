@@ -16,6 +16,7 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kTinyScale = 1.17549435e-38f;  // 2^-126: its reciprocal is still finite
+constexpr float kLowMean = 0x1p-100f, kHighMean = 3.4028235e38f;
 
 // maximum that keeps a NaN of either side (fmaxf drops it)
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -98,7 +99,7 @@ rms_norm_kernel(const T* x, const T* residual, const T* weight, int64_t rows, in
                 T* h, T* y, uint8_t* q, float* scale, float* rstd_out) {
   constexpr int N = Vec<T>::kN;
   constexpr int kRows = TPR == 32 ? 4 : 1;
-  __shared__ float sh_sum[32], sh_big[32], sh_max[32];
+  __shared__ float sh_sum[32], sh_again[32], sh_max[32];
   pdl_wait();
   pdl_launch_dependents();
   const int t = threadIdx.x % TPR;
@@ -137,21 +138,26 @@ rms_norm_kernel(const T* x, const T* residual, const T* weight, int64_t rows, in
   }
   if constexpr (NORM) {
     ss = row_reduce<TPR>(ss, sh_sum, Add());
-    float rstd = 1.f / sqrtf(ss / (float)d + eps);
-    if (ss > 3.4028235e38f) {
-      // the squares of values from 2^64 / sqrt(d) on sum beyond fp32: the whole row once
-      // more, scaled by 2^-80 (eps is nothing beside such a sum). A true infinity stays one
-      constexpr float kDown = 8.271806125530277e-25f;
+    const float mean = ss / (float)d + eps;
+    // y = h a r weight, and rstd = a r: of the smallest rows it is beyond fp32, and y is not
+    float a = 1.f, r = 1.f / sqrtf(mean), rstd = r;
+    if (mean < kLowMean || mean > kHighMean) {
+      // the squares underflow (each is off by up to 2^-150, half of fp32's smallest step: not
+      // seen in a mean of 2^-100) or sum beyond fp32: the whole row once more, scaled by a
+      // power of two. A true infinity stays one
+      const float up = mean < kLowMean ? 0x1p100f : 0x1p-80f;
       ss = 0.f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          const float s = f[i][j] * kDown;
+          const float s = f[i][j] * up;
           ss = fmaf(s, s, ss);
         }
-      ss = row_reduce<TPR>(ss, sh_big, Add());
-      rstd = kDown / sqrtf(ss / (float)d);
+      ss = row_reduce<TPR>(ss, sh_again, Add());
+      r = 1.f / sqrtf(ss / (float)d + eps * up * up);
+      rstd = r * up;
+      if (up > 1.f) a = up; else r = rstd;
     }
     if (t == 0 && rstd_out) rstd_out[row] = rstd;
 #pragma unroll
@@ -162,7 +168,7 @@ rms_norm_kernel(const T* x, const T* residual, const T* weight, int64_t rows, in
       for (int j = 0; j < N; ++j) w[j] = 1.f;
       if (weight && v < nv) unpack(reinterpret_cast<const uint4*>(weight)[v], w);
 #pragma unroll
-      for (int j = 0; j < N; ++j) f[i][j] = f[i][j] * rstd * w[j];
+      for (int j = 0; j < N; ++j) f[i][j] = f[i][j] * a * r * w[j];
       if (y && v < nv) reinterpret_cast<uint4*>(y + at)[v] = pack(f[i]);
     }
   }
@@ -348,7 +354,7 @@ rms_norm_backward_kernel(const T* dy, const T* h, const float* rstd, const T* we
 #pragma unroll
       for (int i = 0; i < WPR; ++i) dot += sh_dot[grp * WPR + i];
     }
-    const float c = -rs * (dot / (float)d);
+    const float c = -dot / (float)d;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = t + i * kGroupThreads;
@@ -362,7 +368,7 @@ rms_norm_backward_kernel(const T* dy, const T* h, const float* rstd, const T* we
         if (dh) unpack(sdh[v], o);
 #pragma unroll
         for (int j = 0; j < N; ++j)
-          o[j] = fmaf(rs, fmaf(x[j], c, weight ? g[j] * wf[j] : g[j]), o[j]);
+          o[j] = fmaf(rs, fmaf(x[j] * rs, c, weight ? g[j] * wf[j] : g[j]), o[j]);
         __stcs(reinterpret_cast<uint4*>(dx + row * d) + v, pack(o));
       }
     }

@@ -333,7 +333,10 @@ typedef enum {
  * x, residual (NULL: none), weight [d] (NULL: ones) in dtype. Outputs: h [T, d] in dtype
  * (non-NULL exactly when there is a residual), y [T, d] in dtype and / or q [T, d] with
  * scale [T] fp32 (y, or q and scale, may be NULL, not all), rstd [T] fp32 (may be NULL).
- * A row that holds a NaN, or an infinity, is NaN in y, q and scale where the formula is. */
+ * A row that holds a NaN, or an infinity, is NaN in y, q and scale where the formula is. The
+ * mean of squares is taken without underflow or overflow, whatever the row's size and eps >= 0;
+ * only with eps = 0 can rstd itself be beyond fp32 (rows below 2^-128): it is then infinite, y
+ * is what the formula gives, and the row has no gradient. */
 NMOE_API nmoe_status nmoe_rms_norm(const void* x, const void* residual, const void* weight,
                                    int64_t T, int64_t d, float eps, nmoe_dtype dtype, void* h,
                                    void* y, void* q, float* scale, float* rstd,

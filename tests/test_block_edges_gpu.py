@@ -6,9 +6,92 @@ import pytest
 import torch
 
 import diffusion_transformer_moe_b200 as nm
-from tests.test_block_gpu import (BF, E4M3, F32, clean, gen, randn)
+from tests.test_block_gpu import (BF, E4M3, F32, NORM32, U, clean, gen, half, norm_ref, randn,
+                                  within)
 
 pytestmark = pytest.mark.gpu
+
+
+def last_step(dtype):
+    """Half a step of the type's subnormals."""
+    f = torch.finfo(dtype)
+    return f.tiny * f.eps / 2
+
+
+# ---- norm ---------------------------------------------------------------------------------
+
+# a row's size and eps: squares that underflow in part or altogether, that sum just below and
+# just above fp32's largest value, or beyond it; eps that is nothing beside them, or as large
+ROWS = [(1e-19, 0.0), (1e-20, 0.0), (1e-21, 1e-42), (1e-25, 0.0), (1e-30, 0.0), (1e-37, 0.0),
+        (1.0, 0.0), (7e17, 0.0), (8e17, 0.0), (9e17, 0.0), (3e18, 1e37), (1e30, 0.0),
+        (1e30, 1e38), (2e37, 0.0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,d", [(2, 8), (3, 520), (2, 2056), (1, 16384), (1300, 512)])
+@pytest.mark.parametrize("size,eps", ROWS)
+def test_norm_of_rows_whose_squares_leave_fp32(T, d, dtype, size, eps):
+    x = extreme_rows(T, d, dtype, size, 1)
+    w = randn(gen(d), d, dtype=dtype)
+    n = nm.rms_norm(x, w, eps=eps, out="both")
+    clean()
+    rstd, y = norm_ref(x, w, float(torch.tensor(eps)))
+    within(n.rstd, rstd, rstd * NORM32 + last_step(F32), "rstd")
+    within(n.y, y, y.abs() * (half(dtype) + 1.01 * NORM32) + last_step(dtype), "y")
+    held = n.q.double() * n.scale.double()[:, None]
+    within(held, y, y.abs() * (half(E4M3) + 3 * NORM32) + n.scale.double()[:, None] * 2.0 ** -10,
+           "q")
+    dy, dh = randn(gen(2), T, d, dtype=dtype), randn(gen(3), T, d, dtype=dtype, scale=1 / size)
+    dx, dw = nm.rms_norm_backward(dy, x, n.rstd, w, dh=dh)
+    clean()
+    r = n.rstd.double()[:, None]
+    xh, g = x.double() * r, dy.double() * w.double()
+    want = r * (g - xh * (g * xh).mean(1, keepdim=True)) + dh.double()
+    mag = r * (g.abs() + xh.abs() * (g * xh).abs().mean(1, keepdim=True)) + dh.double().abs()
+    within(dx, want, want.abs() * half(dtype) + mag * (85 + 8) * U + 4 * last_step(dtype), "dx")
+    prod = dy.double() * xh
+    within(dw, prod.sum(0), prod.abs().sum(0) * (T + 64) * U, "dweight")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,d", [(2, 64), (2, 520), (1300, 512)])
+def test_norm_of_the_largest_and_the_smallest_rows(T, d, dtype):
+    sign = torch.where(torch.rand(T, d, device="cuda", generator=gen(1)) < 0.5, -1.0, 1.0)
+    # rstd is subnormal: half its step is 2^-150 of a value of 2^-128 or more
+    x = (3e38 * sign).to(dtype)
+    n = nm.rms_norm(x, eps=0.0, out="both")
+    clean()
+    rstd, y = norm_ref(x, None, 0.0)
+    within(n.rstd, rstd, rstd * NORM32 + last_step(F32), "rstd")
+    within(n.y, y, y.abs() * (half(dtype) + NORM32 + 2.0 ** -21), "y")
+    # 1 / rms is beyond fp32, and rstd infinite; y is still what it is
+    x = (1e-40 * sign).to(dtype)
+    n = nm.rms_norm(x, eps=0.0, out="both")
+    clean()
+    assert bool((x != 0).all()) and bool((n.rstd == float("inf")).all())
+    _, y = norm_ref(x, None, 0.0)
+    within(n.y, y, y.abs() * (half(dtype) + NORM32), "y")
+    # the formula's 0 / 0
+    n = nm.rms_norm(torch.zeros_like(x), eps=0.0)
+    clean()
+    assert bool(n.y.isnan().all())
+
+
+def test_norm_gradient_of_a_row_that_is_zero_in_part():
+    # the mean of g xhat times rstd is beyond fp32; where h is 0 the gradient is rstd g
+    d = 520
+    h = torch.zeros(3, d, device="cuda")
+    h[:, ::2] = 1e-37
+    dy = torch.ones(3, d, device="cuda")
+    dy[:, ::2] = 50.0
+    rstd = nm.rms_norm(h, eps=0.0).rstd
+    dx, _ = nm.rms_norm_backward(dy, h, rstd)
+    clean()
+    r = rstd.double()[:, None]
+    xh = h.double() * r
+    want = r * (dy.double() - xh * (dy.double() * xh).mean(1, keepdim=True))
+    mag = r * (dy.double() + xh * (dy.double() * xh).mean(1, keepdim=True))
+    within(dx, want, want.abs() * half(F32) + mag * (85 + 8) * U)
 
 
 # ---- 8-bit rows ---------------------------------------------------------------------------
