@@ -27,6 +27,10 @@ ROWS = [(1e-19, 0.0), (1e-20, 0.0), (1e-21, 1e-42), (1e-25, 0.0), (1e-30, 0.0), 
         (1e30, 1e38), (2e37, 0.0)]
 
 
+def extreme_rows(T, d, dtype, size, seed):
+    return randn(gen(seed + d), T, d, dtype=F32, scale=size).to(dtype)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("T,d", [(2, 8), (3, 520), (2, 2056), (1, 16384), (1300, 512)])
 @pytest.mark.parametrize("size,eps", ROWS)
