@@ -98,6 +98,7 @@ struct Cfg {
       MODE == kGemm2 ? 32 * 128 : (SPLIT ? 2 * 32 * 64 : 32 * 64);
   static constexpr size_t kSmem = kRingBytes + kEpiWarps * kEpiStage + 1024;
   static_assert(kSmem <= 232448, "dynamic shared memory beyond the 227 KB a CTA may use");
+  static_assert(tmem_alone(kSmem), "all TMEM columns beside another kernel's");
 };
 
 struct Params {
@@ -673,6 +674,7 @@ struct PairCfg {
   static constexpr size_t kSmem =
       (size_t)kStages * kStageBytes + kPairEpiWarps * kPairEpiStage + 1024;
   static_assert(kSmem <= 232448, "dynamic shared memory beyond the 227 KB a CTA may use");
+  static_assert(tmem_alone(kSmem), "all TMEM columns beside another kernel's");
 };
 
 template <bool SPLIT>

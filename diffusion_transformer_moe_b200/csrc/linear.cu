@@ -587,7 +587,7 @@ linear_tile_kernel(const __grid_constant__ TileArgs<NP> args) {
   const int kb1 = (p.nk * (rank + 1)) >> p.split_log2;
   const int b_bytes = p.bn * kRowBytes;
   const int stage_bytes = kTile128 + b_bytes;
-  const uint32_t tmem_cols = p.bn < 32 ? 32u : (uint32_t)p.bn;
+  const uint32_t tmem_cols = p.bn < 32 ? 32u : (uint32_t)p.bn;  // 128 at most (tmem_alone)
 
   // One k-block's copies, each operand's by one thread (the first one's announces both).
   auto fetch_a = [&](int kb, int stage) {
@@ -878,6 +878,7 @@ constexpr int kAccCols = 256;
 constexpr size_t kPairSmem =
     (size_t)kPairStages * kPairStageBytes + kPairEpiWarps * kPairEpiStage + 1024;
 static_assert(kPairSmem <= kMaxSmem, "dynamic shared memory beyond the 227 KB a CTA may use");
+static_assert(tmem_alone(kPairSmem), "all TMEM columns beside another kernel's");
 
 constexpr int kMaxPairs = 80;
 
@@ -1426,8 +1427,10 @@ bool tile_problem(const Product& g, bool swap, int bn, int split, int sm_count, 
   const int stage_bytes = kTile128 + bn * kRowBytes;
   p->stages = tile_stages(bn, takes_long_ring(tiles, p->nk, bn, split, sm_count));
   const size_t acc = (size_t)4 * (swap ? (size_t)bn * 132 : (size_t)128 * (bn + 4));
-  const size_t ring = (size_t)p->stages * stage_bytes;
-  *smem = (ring > acc ? ring : acc) + 1024;
+  size_t need = (size_t)p->stages * stage_bytes;
+  if (acc > need) need = acc;
+  if (need < kTmemLeastSmem) need = kTmemLeastSmem;  // (rings of narrow tiles: 80 KB)
+  *smem = need + 1024;
   return true;
 }
 

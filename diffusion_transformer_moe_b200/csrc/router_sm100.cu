@@ -43,6 +43,8 @@ constexpr int kStages = 6;
 constexpr int kABytes = kBM * kBK * 2;     // 16 KB
 constexpr int kBBoxBytes = 64 * kBK * 2;   // 8 KB: 64 experts x 64 k
 constexpr int kMaxE = 128;
+// (the least the launch below asks for: one box of experts a stage)
+static_assert(tmem_alone(kStages * (kABytes + kBBoxBytes)), "all TMEM columns beside another's");
 constexpr int kSplit = 2;   // CTAs per token tile (one cluster), each owning half of d
 constexpr int kChunkKB = 2; // k-blocks accumulated per TMEM chunk slice (128-long chunks)
 constexpr uint64_t kDrainNs = 20000000ull;  // 20 ms per drain wait after an abort

@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <stddef.h>
 #include <stdint.h>
 
 namespace nmoe {
@@ -244,6 +245,20 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 }
 
 // ---- tcgen05 ------------------------------------------------------------------------------
+
+// An allocation of TMEM columns waits, without any limit, until the SM has them. CTAs of two
+// clusters that wait for one another's columns on two SMs would wait for good, and so would a
+// CTA for columns of one that waits for its grid to end. So no two CTAs whose columns together
+// exceed an SM's 512 may share one, and shared memory sees to that: every kernel here that
+// allocates asks for kTmemLeastSmem or more, and one that takes more than 128 columns for so
+// much that it and any other of them exceed an SM's (tmem_alone). At most two of kTmemLeastSmem
+// then share an SM. Each CTA costs 1 KB beside what it asks for.
+constexpr size_t kSmSmem = 233472;
+constexpr size_t kTmemLeastSmem = 98304;
+constexpr bool tmem_alone(size_t dynamic_smem) {
+  return dynamic_smem + 1024 + kTmemLeastSmem + 1024 > kSmSmem;
+}
+static_assert(3 * (kTmemLeastSmem + 1024) > kSmSmem, "three CTAs of 128 columns and one more");
 
 // Allocates `ncols` TMEM columns (power of two >= 32); the whole warp must call it. The
 // base address is written to *dst (shared memory).
