@@ -198,6 +198,16 @@ __device__ __forceinline__ uint2 residual4(const Epi& e, int64_t row, int col) {
   return *reinterpret_cast<const uint2*>(e.residual + row * e.cols + col);
 }
 
+__device__ __forceinline__ float4 abs4(float4 v) {
+  return make_float4(fabsf(v.x), fabsf(v.y), fabsf(v.z), fabsf(v.w));
+}
+__device__ __forceinline__ float min4(float4 v) {
+  return fminf(fminf(v.x, v.y), fminf(v.z, v.w));
+}
+__device__ __forceinline__ float max4(float4 v) {
+  return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+}
+
 // What the epilogue adds or multiplies in columns col .. col+3 (inside the output), as
 // loaded and as used.
 struct RawTerms {
@@ -206,6 +216,7 @@ struct RawTerms {
 };
 struct ColTerms {
   float bias[4], scale[4];
+  float lo, hi;  // the scales' least and largest magnitude
 };
 template <bool F8>
 __device__ __forceinline__ RawTerms raw_terms(const Epi& e, int col) {
@@ -220,6 +231,8 @@ __device__ __forceinline__ ColTerms column_terms(const RawTerms& r) {
   ColTerms t;
   unpack4(r.bias, t.bias);
   t.scale[0] = r.scale.x; t.scale[1] = r.scale.y; t.scale[2] = r.scale.z; t.scale[3] = r.scale.w;
+  t.lo = min4(abs4(r.scale));
+  t.hi = max4(abs4(r.scale));
   return t;
 }
 
@@ -231,6 +244,28 @@ enum EpiKind {
   kAny      // activations and pre-activations too
 };
 
+// An accumulator times x_scale w_scale. One product of the scales serves as long as all of a
+// thread's or warp's are normal numbers. Where both are small or both large, their product may
+// leave fp32 though the result does not: they are then applied one after the other (the first
+// step is no further out than the result; of a small and a large one the product lies between).
+// That test is one a row and four columns, or one a tile and warp: one a value made pairs of
+// 8192 x 256 x 2048 28 us, not 18.
+__device__ __forceinline__ bool scales_fit(float row_lo, float row_hi, float col_lo,
+                                           float col_hi) {
+  return row_lo * col_lo >= 1.17549435e-38f && row_hi * col_hi <= 3.4028235e38f;
+}
+// The same over a warp's rows (one a lane) and columns (four a lane); the order of positive
+// floats is that of their bits.
+__device__ __forceinline__ bool warp_scales_fit(float row, float4 cols) {
+  constexpr uint32_t kAll = 0xffffffffu;
+  const float4 c = abs4(cols);
+  const uint32_t r = __float_as_uint(fabsf(row));
+  return scales_fit(__uint_as_float(__reduce_min_sync(kAll, r)),
+                    __uint_as_float(__reduce_max_sync(kAll, r)),
+                    __uint_as_float(__reduce_min_sync(kAll, __float_as_uint(min4(c)))),
+                    __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(max4(c)))));
+}
+
 // Finishes the fp32 accumulators of R rows row0, row0 + step, ... and columns col .. col+3,
 // and stores those below `rows` and inside the output. Everything read is passed in: a load
 // behind the store of the row before would wait for its own round trip.
@@ -241,9 +276,18 @@ __device__ __forceinline__ void finish(const Epi& e, float (&v)[4 * R], const ui
   const bool inside = col < e.cols;
   if constexpr (KIND != kPlain) {
 #pragma unroll
-    for (int i = 0; i < 4 * R; ++i)
-      v[i] = F8 ? fmaf(v[i], row_scale[i / 4] * t.scale[i % 4], t.bias[i % 4])
-                : v[i] + t.bias[i % 4];
+    for (int i = 0; i < R; ++i) {
+      const float rs = row_scale[i];
+      if (F8 && !scales_fit(fabsf(rs), fabsf(rs), t.lo, t.hi)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[4 * i + j] = v[4 * i + j] * rs * t.scale[j] + t.bias[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[4 * i + j] = F8 ? fmaf(v[4 * i + j], rs * t.scale[j], t.bias[j])
+                            : v[4 * i + j] + t.bias[j];
+      }
+    }
     if (KIND == kAny && e.preact) {
 #pragma unroll
       for (int i = 0; i < R; ++i)
@@ -306,8 +350,17 @@ __device__ __forceinline__ void add_residual32(float (&v)[32], const uint4 (&r)[
 // x 2048 with SiLU 30.4 -> 33.8 us).
 template <bool F8>
 __device__ __forceinline__ void add_bias32(const Epi& e, uint2 bias, float (&v)[32],
-                                           float row_scale, int col, int round) {
-  if (F8) {
+                                           float row_scale, bool fit, int col, int round) {
+  if (F8 && !fit) {
+#pragma unroll 1
+    for (int j = 0; j < 32; ++j) {
+      float s = 1.f;
+      if (col + j < e.cols) s = e.col_scale[col + j];
+      // (a loop over registers would spill them: every value is scaled where it is the j-th)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = i == j ? v[i] * row_scale * s : v[i];
+    }
+  } else if (F8) {
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       float4 s = make_float4(1, 1, 1, 1);
@@ -638,7 +691,6 @@ linear_tile_kernel(const __grid_constant__ TileArgs<NP> args) {
   const int64_t lane_row = (int64_t)ta * 128 + q * 32 + lane;
   const int rounds = p.bn / 64, col0 = tb * p.bn + (warp >> 2) * 32 * rounds;
   uint4 res32[4];
-  uint2 bias32 = make_uint2(0, 0);
   float rs32 = 1.f;
   constexpr int kRows = SWAP ? 2 : 4;               // rows a thread finishes at a time
   const int64_t row0 = SWAP ? (int64_t)tb * p.bn : (int64_t)ta * 128;
@@ -666,7 +718,7 @@ linear_tile_kernel(const __grid_constant__ TileArgs<NP> args) {
       rs[i] = 1.f;
     }
   } else if (whole) {
-    bias32 = raw_terms<false>(p.epi, col0 + 4 * lane).bias;
+    raw = raw_terms<F8>(p.epi, col0 + 4 * lane);
     if (F8 && lane_row < p.epi.rows) rs32 = p.epi.row_scale[lane_row];
     load_residual32(p.epi, lane_row, col0, res32);
   } else {
@@ -765,6 +817,7 @@ linear_tile_kernel(const __grid_constant__ TileArgs<NP> args) {
   if (whole) {
     if (!aborted) {
       // (every copy was consumed by an MMA that has completed)
+      const bool fit = !F8 || warp_scales_fit(rs32, raw.scale);
 #pragma unroll 1
       for (int r = 0; r < rounds; ++r) {
         const int c32 = col0 + 32 * r;
@@ -775,7 +828,7 @@ linear_tile_kernel(const __grid_constant__ TileArgs<NP> args) {
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(y[i]);
-        if constexpr (KIND != kPlain) add_bias32<F8>(p.epi, bias32, v, rs32, c32, r);
+        if constexpr (KIND != kPlain) add_bias32<F8>(p.epi, raw.bias, v, rs32, fit, c32, r);
         if constexpr (KIND == kAny) {
           if (p.epi.preact)
             store_row32(p.epi.preact, false, v, lane_row, p.epi.rows, c32, p.epi.cols);
@@ -1137,8 +1190,7 @@ linear_pair_kernel(const __grid_constant__ PairArgs<NP> p) {
       const int row_base = it.m * 256 + (int)rank * 128 + q * 32;
       const int64_t row = (int64_t)row_base + lane;
       const float rs = F8 && row < epi.rows ? epi.row_scale[row] : 1.f;
-      const uint2 bias =
-          KIND != kPlain ? raw_terms<false>(epi, col0 + 4 * lane).bias : make_uint2(0, 0);
+      const RawTerms raw = KIND != kPlain ? raw_terms<F8>(epi, col0 + 4 * lane) : RawTerms();
       uint4 res[4];
       if (KIND != kPlain) load_residual32(epi, row, col0, res);
       int w = 1;
@@ -1147,6 +1199,7 @@ linear_pair_kernel(const __grid_constant__ PairArgs<NP> p) {
       tc_fence_after();
       const uint32_t taddr =
           tmem_base + ((uint32_t)(q * 32) << 16) + acc * kAccCols + part * rounds * 32;
+      const bool fit = !F8 || warp_scales_fit(rs, raw.scale);
 #pragma unroll 1
       for (int r = 0; r < rounds; ++r) {
         const int col = col0 + 32 * r;
@@ -1162,7 +1215,7 @@ linear_pair_kernel(const __grid_constant__ PairArgs<NP> p) {
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(y[i]);
-        if constexpr (KIND != kPlain) add_bias32<F8>(epi, bias, v, rs, col, r);
+        if constexpr (KIND != kPlain) add_bias32<F8>(epi, raw.bias, v, rs, fit, col, r);
         if constexpr (KIND == kAny) {
           if (epi.preact) {
             store_rows32(v, &m.pre, stage0 + buf * kPairEpiHalf, false, one_block, col, row_base,

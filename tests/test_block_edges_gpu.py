@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import diffusion_transformer_moe_b200 as nm
-from tests.test_block_gpu import (BF, E4M3, F32, NORM32, U, clean, gen, half, norm_ref, randn,
-                                  within)
+from tests.test_block_gpu import (BF, E4M3, F32, NORM32, U, clean, gen, half, norm_ref,
+                                  product_error, randn, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,54 @@ def test_codes_of_rows_with_infinities():
     assert float(scale[1]) == float("inf") and bool(scale[2].isnan())
     assert torch.equal(got.isnan(), want.isnan())
     assert bool((got[1].nan_to_num(0) == 0).all()) and bool(got[3].isfinite().all())
+
+
+# ---- products -------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 16, 24), (60, 1008, 264), (200, 144, 136),
+                                   (130, 4096, 64), (4700, 144, 2056)])
+@pytest.mark.parametrize("bias", [False, True])
+def test_scales_whose_product_leaves_fp32(M, K, N, bias):
+    g = gen(M + N)
+
+    def codes(rows):  # +-2^-9 .. 4 2^-9: sums of K products stay below K 2^-14
+        v = torch.randint(1, 5, (rows, K), device="cuda", generator=g) * 2.0 ** -9
+        sign = torch.rand(rows, K, device="cuda", generator=g) < 0.5
+        return torch.where(sign, -v, v)
+
+    a, b = codes(M), codes(N)
+    a[::3] = 0                                     # sums of 0 times whatever the scales are
+    sizes = torch.tensor([1e-30, 1e-10, 1.0, 1e20, 1e30, 2.0 ** -126], device="cuda")
+    sx = sizes[torch.arange(M, device="cuda") % 6].contiguous()
+    sw = (sizes * 0.5)[torch.arange(N, device="cuda") // 3 % 6].contiguous()
+    far = (sx[:, None].double() * sw.double()) > 1e39     # only rows of 0 may meet these
+    a[(far.any(1))] = 0
+    bb = randn(g, N) if bias else None
+    out = nm.linear_fp8(a.to(E4M3), sx, b.to(E4M3), sw, bb, out_f32=True)
+    clean()
+    x, w = a.double() * sx.double()[:, None], (b.double() * sw.double()[:, None]).t()
+    z = x @ w
+    err = product_error(x, w) + z.abs() * 3 * U
+    if bias:
+        z = z + bb.double()
+    within(out, z, err + z.abs() * U + 2 * last_step(F32), "out")
+
+
+@pytest.mark.parametrize("M,K,N", [(3, 32, 24), (200, 160, 136), (4700, 144, 2056)])
+def test_small_and_large_scales_of_one_product(M, K, N):
+    # both small: their product is subnormal or 0, the result is not; both large: it is beyond
+    # fp32, the result is not
+    g = gen(M)
+    for sizes, code in (((2e-25, 3e-15), 384.0), ((2e-22, 3e-24), 448.0), ((2e21, 3e18), 2.0 ** -9),
+                        ((1e-38, 2e30), 1.0), ((2.0 ** 119, 2.0 ** -126), 448.0)):
+        a = (code * (1 - 2 * torch.randint(0, 2, (M, K), device="cuda", generator=g))).float()
+        b = torch.full((N, K), code, device="cuda")
+        b[:, 5:] = 0
+        sx = torch.full((M,), sizes[0], device="cuda")
+        sw = torch.full((N,), sizes[1], device="cuda")
+        out = nm.linear_fp8(a.to(E4M3), sx, b.to(E4M3), sw, out_f32=True)
+        clean()
+        x, w = a.double() * sx.double()[:, None], (b.double() * sw.double()[:, None]).t()
+        z = x @ w
+        within(out, z, product_error(x, w) + z.abs() * 3 * U + last_step(F32), str(sizes))
