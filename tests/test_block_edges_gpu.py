@@ -6,8 +6,8 @@ import pytest
 import torch
 
 import diffusion_transformer_moe_b200 as nm
-from tests.test_block_gpu import (BF, E4M3, F32, NORM32, U, clean, gen, half, norm_ref,
-                                  product_error, randn, within)
+from tests.test_block_gpu import (BF, E4M3, F32, FP8_SHAPES, NORM32, U, check_linear, clean, gen,
+                                  half, norm_ref, product_error, randn, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -181,3 +181,18 @@ def test_small_and_large_scales_of_one_product(M, K, N):
         x, w = a.double() * sx.double()[:, None], (b.double() * sw.double()[:, None]).t()
         z = x @ w
         within(out, z, product_error(x, w) + z.abs() * 3 * U + last_step(F32), str(sizes))
+
+
+@pytest.mark.parametrize("M,K,N", FP8_SHAPES)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("f32", [False, True])
+def test_linear_fp8_with_the_other_activations(M, K, N, act, f32):
+    g = gen(M + K + N + 1)
+    qx, sx = nm.quantize_rows(randn(g, M, K))
+    qw, sw = nm.quantize_rows(randn(g, N, K, scale=K ** -0.5))
+    b, r = randn(g, N), randn(g, M, N)
+    out = nm.linear_fp8(qx, sx, qw, sw, b, act=act, residual=r, out_f32=f32)
+    clean()
+    x, w = qx.double() * sx.double()[:, None], (qw.double() * sw.double()[:, None]).t()
+    z = x @ w + b.double()
+    check_linear(out, z, product_error(x, w) + z.abs() * 5 * U, act, r, "out")
