@@ -318,7 +318,9 @@ NMOE_API nmoe_status nmoe_forward_noalloc(const void* x, const void* W_r, const 
  * scale a row: the value held is q * scale. */
 
 /* Activation of a matrix product's epilogue: z; z / (1 + e^-z); z * (1 + erf(z / sqrt 2)) / 2;
- * z * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) / 2. */
+ * z * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) / 2. In fp32 the relative error grows on
+ * the lower tails as it would if z were moved by a few of its steps: at z = -6 it is at most
+ * 2e-6 (SiLU) and 1.5e-5 (GELU); values below 2^-126 |z| are 0. */
 typedef enum {
   NMOE_ACT_NONE = 0,
   NMOE_ACT_SILU = 1,

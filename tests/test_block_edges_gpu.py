@@ -2,12 +2,14 @@
 8-bit codes at their borders, scales whose product leaves fp32, and activations far from 0.
 Bounds are derived as in test_block_gpu.py: a rounding is off by half a step."""
 
+import math
+
 import pytest
 import torch
 
 import diffusion_transformer_moe_b200 as nm
-from tests.test_block_gpu import (BF, E4M3, F32, FP8_SHAPES, NORM32, U, check_linear, clean, gen,
-                                  half, norm_ref, product_error, randn, within)
+from tests.test_block_gpu import (BF, E4M3, F32, FP8_SHAPES, NORM32, TINY, U, check_linear,
+                                  clean, gen, half, norm_ref, product_error, randn, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -196,3 +198,44 @@ def test_linear_fp8_with_the_other_activations(M, K, N, act, f32):
     x, w = qx.double() * sx.double()[:, None], (qw.double() * sw.double()[:, None]).t()
     z = x @ w + b.double()
     check_linear(out, z, product_error(x, w) + z.abs() * 5 * U, act, r, "out")
+
+
+def activation_error(z, act):
+    """The relative error of an activation in fp32. An exponential's argument is a product
+    of roundings (half a step each), so its error grows with the argument as it would if z
+    were moved by a few half steps; exponential and reciprocal are off by 2 ulp (2^-22) and
+    one (2^-23), and the products behind them by half a step."""
+    z = z.abs()
+    if act == "silu":      # argument -z log2 e: the constant and the product
+        return z * 2 * U + 8 * U
+    if act == "gelu_tanh":  # 2 u = z (c z^2 + c'): three constants and four products, log2 e
+        return 8 * U * (1.5957692 * (z + 0.044715 * z ** 3)) + 8 * U
+    # x = z / sqrt 2 (two), its square (four), the sum with the fit (one), log2 e (two); the
+    # fit's own 1.2e-7, its Horner steps (ten, of values below 2), the reciprocal's 2 in it
+    # with a slope below 3, in the factor t, the exponential's 4, two products
+    return 9 * U * (z * z / 2 + 1.3) + 1.2e-7 + (20 + 6 + 2 + 4 + 2) * U
+
+
+# few rows over a cluster and in swapped tiles, whole tiles, parts over a cluster, pairs
+@pytest.mark.parametrize("M,K,N", [(8, 64, 4096), (16, 2048, 512), (200, 256, 136),
+                                   (100, 4096, 72), (8192, 64, 2048)])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_activations_hold_their_relative_error_on_both_tails(M, K, N, act):
+    g = gen(M + K)
+    x = torch.zeros(M, K, dtype=BF, device="cuda")
+    x[torch.arange(M), torch.arange(M) % K] = 1.0          # the product is a row of W, exactly
+    w = torch.empty(K, N, device="cuda")
+    w[::2] = 110 * (2 * torch.rand(w[::2].shape, device="cuda", generator=g) - 1)
+    w[1::2] = 6 * torch.randn(w[1::2].shape, device="cuda", generator=g)
+    w = w.to(BF)
+    out = nm.linear(x, w, act=act, out_f32=True)
+    clean()
+    z = w.double()[torch.arange(M, device="cuda") % K]
+    if act == "silu":       # (each without the cancellation of 1 + .. on the lower tail)
+        want = z * torch.sigmoid(z)
+    elif act == "gelu":
+        want = z * torch.special.erfc(-z * 0.5 ** 0.5) / 2
+    else:
+        want = z * torch.sigmoid(math.sqrt(8 / math.pi) * (z + 0.044715 * z ** 3))
+    # an exponential's result below 2^-126 is taken as 0
+    within(out, want, want.abs() * activation_error(z, act) + z.abs() * TINY, act)
