@@ -2,7 +2,23 @@
 // As in api.cu, every check runs on the host before anything is enqueued.
 #include <math.h>
 
+#include <atomic>
+
 #include "block_ops.cuh"
+
+namespace nmoe {
+#ifdef NMOE_DEBUG
+static std::atomic<uint64_t> g_block_wait_ns{kDefaultWaitNs};
+uint64_t block_wait_ns() { return g_block_wait_ns.load(); }
+// Debug build only: the budget of the block operators' waits from now on; with 0 the first
+// wait of every kernel runs out.
+extern "C" __attribute__((visibility("default"))) void nmoe_debug_block_wait_ns(uint64_t ns) {
+  g_block_wait_ns.store(ns);
+}
+#else
+uint64_t block_wait_ns() { return kDefaultWaitNs; }
+#endif
+}  // namespace nmoe
 
 namespace {
 

@@ -16,6 +16,9 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
   return v;
 }
 
+// The budget of each bounded wait of these operators; the debug build may set another.
+uint64_t block_wait_ns();
+
 // Column sums that more than one CTA or cluster computes are left as partial rows
 // [parts, d] fp32 and added up in a fixed order by a second launch (launch_sum_parts), so a
 // result never depends on which CTA ran first.

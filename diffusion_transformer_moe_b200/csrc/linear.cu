@@ -1401,7 +1401,7 @@ cudaError_t launch_pairs(const Product& g, int npairs, unsigned* err, cudaStream
   PairArgs<1> a;
   if (!pair_problem(g, npairs, false, &a.prob[0], &a.map[0])) return cudaErrorInvalidValue;
   a.err = err;
-  a.wait_ns = kDefaultWaitNs;
+  a.wait_ns = block_wait_ns();
   const int pairs = a.prob[0].num_items < npairs ? a.prob[0].num_items : npairs;
   const EpiKind kind = epi_kind(g);
   void (*kernel)(PairArgs<1>) = g.f8 ? (kind == kAny ? linear_pair_kernel<true, 1, kAny>
@@ -1455,7 +1455,7 @@ cudaError_t launch_two(const Product& g0, const Product& g1, int npairs, unsigne
   share_pairs(a.prob[0].num_items, a.prob[0].nk, a.prob[1].num_items, a.prob[1].nk, npairs,
               a.first);
   a.err = err;
-  a.wait_ns = kDefaultWaitNs;
+  a.wait_ns = block_wait_ns();
   return launch_kernel(linear_pair_kernel<false, 2, kPlain>, dim3((unsigned)(2 * npairs)),
                        dim3(kPairThreads), kPairSmem, st, true, 2, a);
 }
@@ -1503,7 +1503,7 @@ cudaError_t launch_tiles(const Product& g, bool swap, int bn, int split, int sm_
   a.sums = nullptr;
   a.dz_rows = 0;
   a.err = err;
-  a.wait_ns = kDefaultWaitNs;
+  a.wait_ns = block_wait_ns();
   const EpiKind kind = epi_kind(g);
   void (*kernel)(TileArgs<1>);
   if (g.f8)
@@ -1557,7 +1557,7 @@ cudaError_t launch_two_tiled(const Product& g0, const Product& g1, const TileCho
   a.dz_rows = M;
   a.dz_cols = (int)N;
   a.err = err;
-  a.wait_ns = kDefaultWaitNs;
+  a.wait_ns = block_wait_ns();
   return launch_kernel(linear_tile_kernel<false, false, 2, kPlain>, dim3((unsigned)grid),
                        dim3(kTileThreads), smem[0] > smem[1] ? smem[0] : smem[1], st, true,
                        (unsigned)c.cluster, a);

@@ -275,7 +275,7 @@ template <typename T, int WPR, int VPT>
 __global__ void __launch_bounds__(kBwdThreads, 1)
 rms_norm_backward_kernel(const T* dy, const T* h, const float* rstd, const T* weight,
                          const T* dh, int64_t rows, int d, T* dx, float* partial, int slots,
-                         int cluster, unsigned* err) {
+                         int cluster, unsigned* err, uint64_t wait_ns) {
   constexpr int N = Vec<T>::kN;
   constexpr int kGroups = kBwdWarps / WPR, kGroupThreads = 32 * WPR;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -324,7 +324,7 @@ rms_norm_backward_kernel(const T* dy, const T* h, const float* rstd, const T* we
   for (int64_t row = first; row < rows; row += step) {
     const float rs = rstd[row];
     // (after a timeout the rows that follow are not fetched, and the call's outputs undefined)
-    ptx::ring_wait(&full_bar[grp][slot], phase, abort_v, kDefaultWaitNs);
+    ptx::ring_wait(&full_bar[grp][slot], phase, abort_v, wait_ns);
     const uint4* sdy = reinterpret_cast<const uint4*>(ring + (size_t)slot * arrays * row_bytes);
     const uint4* sh = sdy + nv;
     const uint4* sdh = sh + nv;
@@ -449,7 +449,7 @@ cudaError_t launch_bwd(const void* dy, const void* h, const float* rstd, const v
                        dim3(kBwdThreads), smem, st, true, (unsigned)cluster,
                        static_cast<const T*>(dy), static_cast<const T*>(h), rstd,
                        static_cast<const T*>(weight), static_cast<const T*>(dh), rows, d,
-                       static_cast<T*>(dx), partial, slots, cluster, err);
+                       static_cast<T*>(dx), partial, slots, cluster, err, block_wait_ns());
 }
 
 template <typename T>
