@@ -15,7 +15,8 @@ A block's step around the expert-choice layer::
     dy, dW_r, _ = linear_backward(dlogits, n.y, W_r)
     dx, dw = rms_norm_backward(dy, n.h, n.rstd, w)
 
-and a dense product in 8 bits::
+(E a multiple of 8: the products' row lengths are, and other router weights need padding), and
+a dense product in 8 bits::
 
     q_w, w_scale = quantize_rows(W.t().contiguous())  # once
     n = rms_norm(x, w, residual=res, out="fp8")
@@ -193,7 +194,7 @@ def linear(x, W, bias=None, act="none", residual=None, out_f32=False, preact=Fal
 
     ``act``: "none", "silu", "gelu" or "gelu_tanh". Returns out [M, N] in bf16 (fp32 with
     ``out_f32``), or with ``preact`` the pair (out, x W + bias in bf16), whose second is
-    what ``linear_backward`` needs of an activation."""
+    what ``linear_backward`` needs of an activation. K and N are multiples of 8."""
     dev = x.get_device()
     if stream is not None or dev < 0 or dev != _device():
         return _elsewhere(linear, stream, x, W, bias, act, residual, out_f32, preact, out)
@@ -217,7 +218,8 @@ def linear_fp8(q_x, x_scale, q_w, w_scale, bias=None, act="none", residual=None,
                out=None, stream=None):
     """act((q_x * x_scale) (q_w * w_scale)^T + bias) + residual: q_x [M, K] and q_w [N, K]
     e4m3 with one fp32 scale a row each (from ``rms_norm`` and ``quantize_rows``), bias [N]
-    and residual [M, N] bf16. Returns out [M, N] in bf16, or fp32 with ``out_f32``."""
+    and residual [M, N] bf16. Returns out [M, N] in bf16, or fp32 with ``out_f32``. K is a
+    multiple of 16, N of 8."""
     dev = q_x.get_device()
     if stream is not None or dev < 0 or dev != _device():
         return _elsewhere(linear_fp8, stream, q_x, x_scale, q_w, w_scale, bias, act, residual,
@@ -244,7 +246,8 @@ def linear_backward(dy, x, W, act="none", preact=None, need_dx=True, need_dW=Tru
                     need_dbias=True, stream=None):
     """(dx [M, K] bf16, dW [K, N] bf16, dbias [N] fp32) of ``linear`` from dy [M, N] bf16
     (which is also the residual's gradient); the ones not needed are None. ``preact`` is
-    what ``linear`` gave, with an activation; without one it is None."""
+    what ``linear`` gave, with an activation; without one it is None. K and N are multiples of
+    8, M is any."""
     dev = dy.get_device()
     if stream is not None or dev < 0 or dev != _device():
         return _elsewhere(linear_backward, stream, dy, x, W, act, preact, need_dx, need_dW,

@@ -381,7 +381,7 @@ struct BalanceGrid {
   bool final;
 };
 BalanceGrid balance_grid(int64_t S, int E, int n_seg) {
-  constexpr int kBlocks = 148;
+  constexpr int kBlocks = 148;  // (not the device's SMs: the sums' order is the same on any)
   const int64_t want = ceil_div(S, kWarps * (E <= 128 ? Batch<4>::kTokens : Batch<8>::kTokens));
   const bool final = S <= kClusterTokens;
   const int64_t most = final ? 8 : kBlocks / n_seg > 1 ? kBlocks / n_seg : 1;

@@ -241,7 +241,7 @@ __device__ __forceinline__ ColTerms column_terms(const RawTerms& r) {
 }
 
 // What an epilogue has to do. The code of what it has not is left out: it cost small products
-// 0.4 us of 2.7 (4 x 1032 x 56), most of it registers that kept the next launch off the SM.
+// 0.4 us of 3.1 (4 x 1032 x 56), most of it registers that kept the next launch off the SM.
 enum EpiKind {
   kPlain,   // bf16 out, nothing added
   kAffine,  // scales, bias, residual, either type
@@ -1566,10 +1566,11 @@ cudaError_t launch_two_tiled(const Product& g0, const Product& g1, const TileCho
 // Estimated times in microseconds: a launch, a k-block's time, an epilogue a wave, for a split
 // the cluster's exchange, and the CTAs that run at one time (clusters of four and eight leave
 // SMs of their group empty). Fits to timings of 170 products (1 to 8192 rows, 64 to 8192 terms,
-// 64 to 6000 columns) on every variant; on 60 others the variant of the smallest estimate took
-// 1% more than the fastest one in the mean and 20% at most. By comparison, pairs alone take up
-// to 4.3 times as long (one row, 8192 x 2048: 38 against 8.8 us) and one-CTA tiles alone 2.4
-// times (2048 x 8192 from 333 terms: 35 against 14 us).
+// 64 to 6000 columns) on every variant; on 100 others the variant of the smallest estimate took
+// 1.6% more than the fastest one in the mean and 40% at most (36 x 1192 x 3688: 9.3 us, 6.6 in
+// swapped tiles over clusters of four). By comparison, pairs alone take up to 4.3 times as long
+// (one row, 8192 x 2048: 38 against 8.8 us) and one-CTA tiles alone 2.4 times (2048 x 8192 from
+// 333 terms: 35 against 14 us).
 double pair_estimate(double items, double k_blocks) {
   return 3.9 + 0.4 * k_blocks + 0.5 * items;
 }
@@ -1711,8 +1712,9 @@ cudaError_t launch_linear_grads(const void* dz, const void* x, const void* W, in
     const int64_t kx = ceil_div(N, 64), kw = ceil_div(M, 64);
     const Product& g0 = kw > kx ? gw : gx;  // the longer one's CTAs first
     const Product& g1 = kw > kx ? gx : gw;
-    // (two launches behind one another take longer than each in its turn; over 230 gradients
-    // the choice took 1% more than the best of the three in the mean and 45% at most)
+    // (two launches behind one another take longer than each in its turn; over 97 gradients the
+    // choice took 1.6% more than the best of the three in the mean and 38% at most: 6228 x 5456
+    // x 152 63 us, as one launch of pairs 45)
     const double apart = 1.1 * (cx.us + cw.us) + 4.0;
     TileChoice tiles = choose_two(g0, g1, 0, 0, sm_count);
     bool beside = false;  // dbias beside the tiles, not 3 us in a launch before them

@@ -420,7 +420,8 @@ NMOE_API size_t nmoe_balance_loss_workspace(int64_t T, int64_t E, int64_t n_segm
 /* Its gradient with respect to the router's logits (counts are held constant: they have no
  * gradient). With g_e = dloss[s] * coef * E * counts[s, e] / (k N^2), a token's row is
  *   p (g - sum_j p_j g_j) for softmax scores, p (1 - p) g for sigmoid scores, 0 if masked,
- * dlogits [T, E] in dtype (fp32, or bf16 as nmoe_linear_backward takes it). dloss
+ * dlogits [T, E] in dtype (fp32, or bf16 as nmoe_linear_backward takes it where E is a multiple
+ * of 8). dloss
  * [n_segments] fp32 (NULL: ones); counts, mask and sizes as in the forward call. */
 NMOE_API nmoe_status nmoe_balance_loss_backward(const float* scores, const uint8_t* mask,
                                                 const int32_t* counts, const float* dloss,
