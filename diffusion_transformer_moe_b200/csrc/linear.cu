@@ -67,7 +67,7 @@ constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 // by 2 and 1 ulp. An exponential's argument is rounded like any product, which moves a value
 // far out on a tail as much as a step or two of z would: SiLU is off by up to (2 |z| + 8) 2^-24
 // of its value, the tanh form by 8 (|2u| + 1) 2^-24, the erf form by 9 (z^2 / 2 + 6) 2^-24 and
-// its fit's 1.2e-7. bf16 outputs are rounded to 2^-9; fp32 outputs show it. An exponential or
+// its fit's 1.2e-7. bf16 outputs are rounded by up to 2^-8; fp32 outputs show it. An exponential or
 // logistic function below 2^-126 counts as 0.
 
 // s = 1 / (1 + e^-t), the logistic function; with z (1 + tanh u) / 2 = z / (1 + e^-2u) it
