@@ -223,10 +223,11 @@ cudaError_t launch_rows(const void* x, const void* residual, const void* weight,
 
 // Rows of up to 256 vectors (2048 bf16, 1024 fp32 values) go to one warp each once there
 // are rows enough for every SM's warps, else to a block of 256 threads: with 512 bf16
-// values, residual and 8-bit output, 1 row takes 1.8 us on a block and 2.0 on a warp, 592
-// rows 2.3 and 2.2, 8192 rows 17 and 5.4. From 129 vectors on the warp's longer rows pay
-// only with the second reduction of an 8-bit output (8192 x 2048 bf16: 25.5 and 25.1 us
-// with it, 19.6 and 20.2 without; 2368 rows: 6.8 and 6.3, 5.4 and 5.4).
+// values, residual and 8-bit output, 1 row takes 1.7 us on a block and 1.95 on a warp, 592
+// rows 2.5 and 2.25, 8192 rows 19 and 7.3. From 129 vectors on the warp's longer rows pay only
+// with the second reduction of an 8-bit output (8192 x 2048 bf16 with a residual: 22.8 and
+// 21.1 us; without an 8-bit output 22.3 and 24.6), and where h and y go out too up to 192 (8192
+// x 1344 22.2 and 17.7 us, 8192 x 2048 26.7 and 27.9, 4000 x 2048 12.7 and 13.5).
 template <typename T, bool NORM>
 cudaError_t launch_rows_of(const void* x, const void* residual, const void* weight, int64_t rows,
                            int d, float eps, void* h, void* y, void* q, float* scale,
@@ -236,7 +237,8 @@ cudaError_t launch_rows_of(const void* x, const void* residual, const void* weig
     return fn(x, residual, weight, rows, d, eps, h, y, q, scale, rstd, st);
   };
   if (nv <= 32) return go(launch_rows<T, 32, 1, NORM>);
-  if (nv <= (q ? 256 : 128) && 16 * rows >= (int64_t)nv * sm_count) {
+  const int longest = !q ? 128 : residual && y ? 192 : 256;
+  if (nv <= longest && 16 * rows >= (int64_t)nv * sm_count) {
     if (nv <= 64) return go(launch_rows<T, 32, 2, NORM>);
     if (nv <= 128) return go(launch_rows<T, 32, 4, NORM>);
     return go(launch_rows<T, 32, 8, NORM>);
